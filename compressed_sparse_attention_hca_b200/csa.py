@@ -630,15 +630,20 @@ def tree_mqa(Q, entries, win, win_start, draft, tree_mask, ctx_len, q_pos, windo
     else:
         _need(dev, Q.dtype, "O", (O,))
     row = c if kv_dt != KV_FP8MIX else row_bytes(kv_dt, c)
-    paged = options is not None and options.entry_pages
-    if (win.shape[0] != B or win.shape[2] != row or win_start.numel() != B or entries.shape[-1] != row or
-            (not paged and entries.shape[:2] != (B, E))):
+    norm_g, table, _ = getattr(options, "_keep", (None, None, None))  # as mqa_options() was given them
+    pg = options.entry_pages.contents if options is not None and options.entry_pages else None
+    if (win.shape != (B, win.shape[1], row) or win_start.numel() != B or entries.shape[-1] != row or
+            (pg is None and entries.shape != (B, E, row))):
         raise ValueError("entries must be [B, E, row] (or a pool of rows), win [B, n, row] and win_start [B]")
-    if D and (tree_mask is None or tree_mask.shape != (B, T, (D + 31) // 32) or draft.shape[0] != B or
-              draft.shape[2] != row):
+    if pg is not None and (entries.numel() < pg.n_pages * pg.page_entries * row or
+                           (table is not None and table._keep.shape[0] < B)):
+        raise ValueError("entries must be a pool of n_pages * page_entries rows and its table have a row per request")
+    if norm_g is not None and (norm_g.dtype is not _F32 or norm_g.numel() != c):
+        raise ValueError("q_norm_g must be float32 [c]")
+    if D and (tree_mask is None or tree_mask.shape != (B, T, (D + 31) // 32) or draft.shape != (B, D, row)):
         raise ValueError("draft must be [B, D, row] and tree_mask [B, T, ceil(D / 32)]")
     if (ctx_len.numel() != B or q_pos.shape != (B, T) or sink.numel() != H or
-            (idx is not None and idx.shape[:2] != (B, T)) or (n_nodes is not None and n_nodes.numel() != B)):
+            (idx is not None and idx.shape != (B, T, k)) or (n_nodes is not None and n_nodes.numel() != B)):
         raise ValueError("ctx_len and n_nodes must be [B], q_pos [B, T], idx [B, T, k], sink [H]")
     if ws is None:
         need = tree_mqa_workspace_size(B, T, H, c, (k if idx is not None else E) + window + D, q_dt, kv_dt, options)
