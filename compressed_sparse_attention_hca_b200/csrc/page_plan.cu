@@ -289,7 +289,7 @@ cudaError_t launch_page_plan(const PagePlanArgs& args, cudaStream_t s) {
     a.maps[i].inv_rows = inverse(a.maps[i].page_rows);
   }
   const size_t smem = (size_t)(a.batch + 1) * (8 * a.n_maps + 12);
-  if (smem > 48 * 1024) {
+  if (smem > 40 * 1024) {  // 48 KB without asking, the kernel's static arrays among them
     const cudaError_t e =
         cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
