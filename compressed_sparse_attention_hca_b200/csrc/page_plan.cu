@@ -12,6 +12,11 @@
 // do not wait for one another; the stack's count, if updated in place,
 // is written by the last CTA to have read it.
 //
+// Places of the table that hold no page (the stack was empty when they were
+// taken) are not given back, so every CTA first counts the pages that are: of a
+// request that gives back a few places the thread that reads its lengths, of
+// one that gives back many all warps, 256 places at a time.
+//
 // Latency bounds it: a step of 256 requests takes 6.5 us (a launch ~2.5, then
 // four or five dependent reads and the scan), 16 prompts of 131,072 to 262,144
 // tokens 11.7 us for 7 MB of slots.  Code comes cold from the instruction cache,
@@ -26,6 +31,8 @@ CSA_DEFINE_STATUS_READER(take_status_page_plan)
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kFew = 4;    // places given back that a thread looks at by itself
+constexpr int kAhead = 8;  // reads of places that a lane has in flight where there are more
 constexpr int64_t kMaxLen = (int64_t)1 << 40;
 
 __device__ __forceinline__ int64_t clamp_len(int64_t n) { return n < 0 ? 0 : min64(n, kMaxLen); }
@@ -62,18 +69,20 @@ struct Sums {
   }
 };
 
-__device__ __forceinline__ Sums sums_of(const PagePlanArgs& a, int b, int* p0_out) {
+// All of a request's sums but the pages given back, which lie in [p1, p0).
+__device__ __forceinline__ Sums sums_of(const PagePlanArgs& a, int b, int* p0_out, int* p1_out) {
   const int64_t before = clamp_len(a.len_before[b]), after = clamp_len(a.len_after[b]);
   const int64_t p0 = min64(pages_of(before, a), a.max_pages), want = pages_of(after, a);
   const int64_t p1 = min64(want, a.max_pages);
   Sums s;
   s.take = (int)max64(0, p1 - p0);
-  s.give = (int)max64(0, p0 - p1);
+  s.give = 0;
   s.want = max64(0, want - p0);
 #pragma unroll
   for (int i = 0; i < kMaxSlotMaps; ++i)
     s.rows[i] = i < a.n_maps ? max64(0, quot(after, a.maps[i].inv_m) - quot(before, a.maps[i].inv_m)) : 0;
   *p0_out = (int)p0;
+  *p1_out = (int)p1;
   return s;
 }
 
@@ -90,24 +99,54 @@ __device__ __forceinline__ int owner(const T* pre, int batch, T x) {
   return lo;
 }
 
+__device__ __forceinline__ bool is_page(const PagePlanArgs& a, int pg) { return (uint32_t)pg < (uint32_t)a.n_pages; }
+// What is neither a page nor the -1 of one that could not be had.
+__device__ __forceinline__ bool is_bad(const PagePlanArgs& a, int pg) { return pg != -1 && !is_page(a, pg); }
+// The k-th place from `at` on that holds a page (`last` if there are fewer).
+__device__ __forceinline__ const int32_t* nth_page(const PagePlanArgs& a, const int32_t* at, const int32_t* last, int k) {
+#pragma unroll 1
+  for (; at < last; ++at)
+    if (is_page(a, *at) && k-- == 0) break;
+  return at;
+}
+
+// Where a thread has got to among a request's places that do not all hold a page.
+struct Cursor {
+  int b = -1, k;  // page k of request b
+  const int32_t* at;
+};
+
 struct Plan {
   const PagePlanArgs& a;
-  const int *take, *give, *p0;  // prefix sums [batch + 1]; pages before [batch]
+  const int *take, *give;  // prefix sums [batch + 1] of places taken and pages given back
+  const int *p0, *p1;      // pages before and after [batch]
   int count, R;
+  // The page at `at`, -1 where there is none.
   __device__ __forceinline__ int checked(const int32_t* at) const {
     if (at == nullptr) return -1;
     const int pg = *at;
-    if (pg >= 0 && pg < a.n_pages) return pg;
-    flag_status(kStatusBadPage);
+    if (is_page(a, pg)) return pg;
+    if (pg != -1 || (at >= a.free_list && at < a.free_list + a.n_pages)) flag_status(kStatusBadPage);
     return -1;
+  }
+  // The place of the i-th page given back.
+  __device__ __forceinline__ const int32_t* given(int i, Cursor& c) const {
+    const int b = owner(give, a.batch, i), k = i - give[b], n = p0[b] - p1[b];
+    const int32_t* const row = a.table + (int64_t)b * a.max_pages + p1[b];
+    if (give[b + 1] - give[b] == n) return row + k;
+    const bool on = c.b == b && c.k < k;
+    c.at = nth_page(a, on ? c.at + 1 : row, row + n - 1, on ? k - c.k - 1 : k);
+    c.b = b;
+    c.k = k;
+    return c.at;
   }
   // Where the number of page i of the pages taken is read: in the stack, or in
   // the table slot of the page given back that this call puts there; nullptr
   // when the stack is empty by then.
   __device__ __forceinline__ const int32_t* taken(int64_t i) const {
     if (i < R) {
-      const int b = owner(give, a.batch, (int)i);
-      return a.table + (int64_t)b * a.max_pages + p0[b] - (give[b + 1] - give[b]) + ((int)i - give[b]);
+      Cursor c;
+      return given((int)i, c);
     }
     const int64_t at = (int64_t)count + R - 1 - i;
     return at < 0 ? nullptr : a.free_list + at;
@@ -181,20 +220,69 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs a) {
   int* take = reinterpret_cast<int*>(row_pre + (int64_t)a.n_maps * (a.batch + 1));
   int* give = take + a.batch + 1;
   int* p0 = give + a.batch + 1;
+  int* p1 = p0 + a.batch;
   __shared__ Sums warp_sums[kThreads / 32];
   __shared__ int64_t want_total;
+  __shared__ int n_long;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) n_long = 0;
+  __syncthreads();
   after_previous();
   const int c0 = *a.count;
   const int count = (int)max64(0, min64(c0, a.n_pages));
 
-  // exclusive prefix sums: a run of requests per thread, then lanes, then warps
+  // the sums of a run of requests per thread; give[b]: the pages that b gives back
   const int per = (a.batch + kThreads - 1) / kThreads;
   const int b0 = min(a.batch, tid * per), b1 = min(a.batch, b0 + per);
   Sums mine{};
-  int p;
+  bool bad = false;
 #pragma unroll 1
-  for (int b = b0; b < b1; ++b) mine.add(sums_of(a, b, &p));
+  for (int b = b0; b < b1; ++b) {
+    mine.add(sums_of(a, b, &p0[b], &p1[b]));
+    const int n = p0[b] - p1[b];
+    int pages = 0;
+    if (n > kFew) {
+      take[atomicAdd(&n_long, 1)] = b;  // a list of them, until the prefix sums replace it
+    } else if (n > 0) {
+      const int32_t* const row = a.table + (int64_t)b * a.max_pages + p1[b];
+      int pg[kFew];
+#pragma unroll
+      for (int j = 0; j < kFew; ++j) pg[j] = row[min(j, n - 1)];
+#pragma unroll
+      for (int j = 0; j < kFew; ++j) {
+        pages += j < n && is_page(a, pg[j]);
+        bad |= is_bad(a, pg[j]);
+      }
+    }
+    give[b] = pages;
+  }
+  __syncthreads();
+  int turn = 0;  // of the warps
+#pragma unroll 1
+  for (int l = 0; l < n_long; ++l) {
+    const int b = take[l];
+    const uint32_t n = (uint32_t)(p0[b] - p1[b]);
+    const int32_t* const row = a.table + (int64_t)b * a.max_pages + p1[b];
+#pragma unroll 1
+    for (uint32_t j0 = 0; j0 < n; j0 += 32 * kAhead, ++turn) {
+      if (turn % (kThreads / 32) != warp) continue;
+      int pg[kAhead], pages = 0;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) pg[u] = row[min(j0 + 32 * u + lane, n - 1)];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        pages += j0 + 32 * u + lane < n && is_page(a, pg[u]);
+        bad |= is_bad(a, pg[u]);
+      }
+      pages = __reduce_add_sync(0xffffffffu, pages);
+      if (lane == 0) atomicAdd(&give[b], pages);
+    }
+  }
+  if (n_long > 0) __syncthreads();
+  if (bad) flag_status(kStatusBadPage);
+  // exclusive prefix sums: over lanes, then warps, then the thread's requests
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine.give += give[b];
   Sums inc = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -210,10 +298,11 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs a) {
   if (lane > 0) run.add(before_lane);
 #pragma unroll 1
   for (int b = b0; b < b1; ++b) {
-    const Sums s = sums_of(a, b, &p);
+    int q0, q1;
+    Sums s = sums_of(a, b, &q0, &q1);
+    s.give = give[b];
     take[b] = run.take;
     give[b] = run.give;
-    p0[b] = p;
     for (int i = 0; i < a.n_maps; ++i) row_pre[i * (a.batch + 1) + b] = run.rows[i];
     run.add(s);
   }
@@ -226,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs a) {
   __syncthreads();
 
   const int A = take[a.batch], R = give[a.batch];
-  const Plan plan{a, take, give, p0, count, R};
+  const Plan plan{a, take, give, p0, p1, count, R};
   const int64_t t0 = (int64_t)blockIdx.x * kThreads + tid, nt = (int64_t)gridDim.x * kThreads;
 #pragma unroll 1
   for (int i = 0; i < a.n_maps; ++i) {
@@ -246,12 +335,11 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs a) {
     const int b = owner(take, a.batch, (int)i);
     a.table[(int64_t)b * a.max_pages + p0[b] + (i - take[b])] = plan.checked(plan.taken(i));
   }
+  Cursor c;
 #pragma unroll 1
   for (int64_t i = t0; i < R; i += nt) {
-    const int b = owner(give, a.batch, (int)i);
-    const int j = p0[b] - (give[b + 1] - give[b]) + ((int)i - give[b]);
     const int64_t at = (int64_t)count + R - 1 - i;
-    if (at < a.n_pages) a.free_list[at] = a.table[(int64_t)b * a.max_pages + j];
+    if (at < a.n_pages) a.free_list[at] = *plan.given((int)i, c);
     else flag_status(kStatusBadPage);
   }
 
@@ -266,9 +354,8 @@ __global__ void __launch_bounds__(kThreads) page_plan_kernel(PagePlanArgs a) {
       last = atomicAdd(a.info + 3, 1) == (int)gridDim.x - 1;
     }
     if (last) {
-      const int64_t left = (int64_t)count + R - A;
       const int got = (int)min64(A, (int64_t)count + R);
-      *a.count_out = (int)max64(0, min64(left, a.n_pages));
+      *a.count_out = (int)min64((int64_t)count + R - got, a.n_pages);
       a.info[0] = got;
       a.info[1] = R;
       a.info[2] = (int)min64(want_total - got, 0x7FFFFFFF);
@@ -288,7 +375,7 @@ cudaError_t launch_page_plan(const PagePlanArgs& args, cudaStream_t s) {
     a.maps[i].inv_m = inverse(a.maps[i].m);
     a.maps[i].inv_rows = inverse(a.maps[i].page_rows);
   }
-  const size_t smem = (size_t)(a.batch + 1) * (8 * a.n_maps + 12);
+  const size_t smem = (size_t)(a.batch + 1) * (8 * a.n_maps + 16);
   if (smem > 40 * 1024) {  // 48 KB without asking, the kernel's static arrays among them
     const cudaError_t e =
         cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

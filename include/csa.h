@@ -596,7 +596,9 @@ typedef struct {
  * page) order i, go to position count + R-1-i; the A pages taken, in
  * (request, page) order j, come from position count + R-1-j; so pages given
  * back by a call are taken first, and shrinking after growing by the same
- * lengths restores the stack.  free_count_out = count + R - A.
+ * lengths restores the stack.  free_count_out = count + R - A.  A page that
+ * could not be had is not among the A, and its place, which holds -1, is not
+ * among the R when the request shrinks.
  *
  *   len_before, len_after  [batch] int64 (device); below 0 counts as 0, above
  *              2^40 as 2^40.
@@ -614,10 +616,12 @@ typedef struct {
  *              before the first use, left zero.  Calls that may overlap must
  *              not share it.
  * A page that could not be had leaves -1 in the table (within max_pages) and
- * -1 in the slot maps; requests are served in order.  A page outside
- * [0, n_pages) in the stack or the table, or a count outside [0, n_pages],
- * touches no memory outside the arrays and csa_check_device_status reports
- * CSA_ERR_INVALID_ARG.  One launch.
+ * -1 in the slot maps, of this step and of later ones that come to its rows;
+ * requests are served in order.  Growing on does not fetch it later: a request
+ * that was short shrinks to the pages that it has (or ends) and grows again.
+ * Any other page outside [0, n_pages) in the table, one in the stack, or a count
+ * outside [0, n_pages], touches no memory outside the arrays, is not given back,
+ * and csa_check_device_status reports CSA_ERR_INVALID_ARG.  One launch.
  * Limits: batch <= 4096, batch * max_pages < 2^31, page_tokens <= 2^20,
  * n_pages * page_tokens / m < 2^31 (and n_pages * 128 with sf_slots).
  */
