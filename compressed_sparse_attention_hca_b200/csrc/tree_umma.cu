@@ -85,6 +85,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 14.f;  // log2 headroom before the maximum is raised (fp16 weights reach 2^16)
 constexpr int kMaxRope = 64;
 constexpr int kMaxSplits = 256;
+constexpr int kFewParts = 16;  // fixed split counts up to this are added by one group of threads
 constexpr int kMaxNodes = 1184;  // nodes of a call whose units are cut evenly (8 units per SM)
 constexpr int kMaxDraft = 1024;
 constexpr int kExpMax = 114;     // |e| of a power of two kept beside fp16 values (they reach 2^15 2^114)
@@ -1451,8 +1452,13 @@ cudaError_t launch_tree_umma(const MqaArgs& a, cudaStream_t s) {
   const cudaError_t e = a.kv_dt == CSA_KV_FP8MIX ? launch_tree<true>(tmQ, t, s) : launch_tree<false>(tmQ, t, s);
   if (e != cudaSuccess || t.p.slots == 0) return e;
   const unsigned octets = (unsigned)(t.p.units * (kHG / 8));
-  return octets >= (unsigned)sm_count_tree()
-             ? launch_overlapped(tree_combine_kernel<1>, octets, kCombineThreads, 0, 1, s, t)
+  // G changes the order of the sums, which a fixed split count promises to be
+  // the same in any batch: there it follows from that count alone.  (The whole
+  // call, G = 1 / 4: 120 units of 2 parts 132 / 147 us, of 16 199 / 205, of 24
+  // 253 / 260; one unit of 2 parts 355 / 355, of 16 59.5 / 57.0, of 24 45.8 /
+  // 41.9, of 128 49.1 / 27.1.)
+  const bool one = t.p.mode == kTreeFixed ? t.p.splits <= kFewParts : octets >= (unsigned)sm_count_tree();
+  return one ? launch_overlapped(tree_combine_kernel<1>, octets, kCombineThreads, 0, 1, s, t)
              : launch_overlapped(tree_combine_kernel<4>, 4 * octets, kCombineThreads, 0, 1, s, t);
 }
 
