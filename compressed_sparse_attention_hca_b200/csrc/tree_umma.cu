@@ -46,7 +46,11 @@
 // two values.  A power of two per row, 2^e, keeps the row in fp16's range, and
 // is put back where it costs nothing: on the row's logits, and in the exponent
 // of its weights.  P' = 2^(s + e - M) then carries it to O^T, M being the
-// maximum of s + e, and the sums take 2^-e P'.  The query is scaled by a power
+// maximum of s + e.  The sums take 2^(s - M): 2^-e P', or of rows so small that
+// P' may have been flushed to 0 where 2^(s - M) counts (e < -18: a row below
+// 2^-3 or so, or of zeros) their logits once more (HCA at 1M with one row in 100
+// of zeros: 280 us against 277).  e is at least -80, so that 2^30 rows of
+// 2^(s - M) <= 2^(14 + 80) stay in fp32's range.  The query is scaled by a power
 // of two per unit likewise.
 //
 // Work split: units are cut where the flattened list of all units' chunks is
@@ -89,6 +93,11 @@ constexpr int kFewParts = 16;  // fixed split counts up to this are added by one
 constexpr int kMaxNodes = 1184;  // nodes of a call whose units are cut evenly (8 units per SM)
 constexpr int kMaxDraft = 1024;
 constexpr int kExpMax = 114;     // |e| of a power of two kept beside fp16 values (they reach 2^15 2^114)
+constexpr int kRowExpMin = -80;  // e of an FP8MIX row: sums of 2^(s - M) reach 2^30 2^14 2^80
+// Below this e the sums take a row's logits again.  At it, P' = 2^(s + e - M) is
+// flushed below 2^-126, so s - M < -108, where the row that sets M has s - M >=
+// -(65 + 14) (its values are below 2^80, its e up to 65): a loss of 2^-29 of the sum.
+constexpr int kRowExpLow = -18;
 
 constexpr int kOffKV = 0;                       // 4 pairs of [128 rows][128 B] atoms: 128 KB
 constexpr int kOffQ = kOffKV + 4 * kPair;       // 8 x [64 heads][128 B]: 64 KB
@@ -115,6 +124,7 @@ struct Misc {
   alignas(16) float mneg[kHG];  // minus the running maximum (0 while there is none)
   alignas(16) float m[kHG];     // running maximum (log2), -inf while there is none
   alignas(16) float corr[kHG];  // rescale factor of a raise; at the end the output factor
+  float root[kHG];              // FP8MIX: its square root, as sums may be 2^94 before a raise by 2^150
   float red[4][kHG];        // per-quadrant maxima, then sums
   float cs[2][kMaxRope / 2], sn[2][kMaxRope / 2];  // RoPE at +t (query) and -t (output)
   // of a chunk, the chunk after and the one after that:
@@ -524,7 +534,7 @@ struct F8Last {
         int e = max(exponent(fmaxf(fabsf(sc[i].x), fabsf(sc[i].y))) + 1 - 7, exponent(tail) + 1 - 15);
         e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
         e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-        e = max(-kExpMax, min(kExpMax, e));
+        e = max(kRowExpMin, min(kExpMax, e));
         const float f = pow2i(-e);
         *reinterpret_cast<uint32_t*>(&ms.scale[buf][r][2 * g]) = pack_f16(sc[i].x * f, sc[i].y * f);
         if (g == 0) ms.rowe[buf][r] = e;
@@ -1104,7 +1114,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float cm = fmaxf(fmaxf(ms.red[0][st], ms.red[1][st]), fmaxf(ms.red[2][st], ms.red[3][st]));
             const float old = ms.m[st];
             const float m = cm > old + kLazy || old == -INFINITY ? fmaxf(cm, old) : old;  // (a NaN stays)
-            ms.corr[st] = old == -INFINITY || m == old ? 1.f : exp2f(old - m);
+            const float down = old == -INFINITY || m == old ? 0.f : old - m;
+            ms.corr[st] = exp2f(down);
+            if (FP8) ms.root[st] = exp2f(0.5f * down);
             ms.m[st] = m;
             ms.mneg[st] = m == -INFINITY ? 0.f : -m;
           }
@@ -1114,7 +1126,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (c > s.c0) {
             // sums and O^T so far (lane = dim; this warp's two slabs)
 #pragma unroll
-            for (int h = 0; h < (FP8 ? 1 : 32); ++h) l[h] *= ms.corr[32 * half + (FP8 ? lane : h)];
+            for (int h = 0; h < (FP8 ? 1 : 32); ++h) {
+              const float r = FP8 ? ms.root[32 * half + lane] : ms.corr[32 * half + h];
+              l[h] *= r;
+              if (FP8) l[h] *= r;
+            }
             tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -1132,12 +1148,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&ms.p_full);
           mbar_arrive(&ms.row_empty[buf]);
         }
+        float back = FP8 ? pow2i(-e) : 1.f;
+        if (FP8 && __any_sync(0xffffffffu, e < kRowExpLow)) {
+          logits();  // they are there until all softmax warps have filled the tile
+          tc_fence_before();
+          back = 1.f;
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const float4 mn = mneg[g];
+            const float m4[4] = {mn.x, mn.y, mn.z, mn.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[4 * g + i] = on ? ex2(fmaf(x[4 * g + i], sc, m4[i])) : 0.f;
+          }
+        }
         // the next chunk, if there is one, into the tile
         role_wait(ms, &ms.row_full[buf_of(chunk + 1)], buf_par(chunk + 1));
         const bool more = ms.more[buf_of(chunk + 1)] != 0;
         if (more) filler.start(ms, st, chunk + 1);
         if (FP8) {
-          const float back = pow2i(-e);
 #pragma unroll
           for (int h = 0; h < 32; ++h) x[h] *= back;
           l[0] += reduce32(x, lane);
@@ -1320,7 +1348,9 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const __g
 #pragma unroll
     for (int i = 0; i < kLane; ++i) {
       if (32 * i >= n) break;
-      float w = !zero && ml[i].x != -INFINITY ? ml[i].y * exp2f(ml[i].x - M) : 0.f;
+      // in two factors, as l may be 2^124 where m - M is below -126
+      const float down = ml[i].x - M;
+      float w = !zero && ml[i].x != -INFINITY ? ml[i].y * exp2f(fmaxf(down, -120.f)) * exp2f(fminf(down + 120.f, 0.f)) : 0.f;
       ml[i].y = w;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);

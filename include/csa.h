@@ -698,6 +698,13 @@ csa_status_t csa_nvfp4_linear(const void* X, const void* X_sf, const void* W, co
  * a sink of -inf gives zeros.  A NaN in a row or query makes the outputs that
  * depend on it NaN, and no others.  Row values stay below 2^80 in magnitude
  * (2^30 rows with weights of up to 2^14 are summed in fp32).
+ * FP8MIX rows on the tensor cores (bf16 Q, dim 512, 64 or 128 heads) are taken
+ * as fp16 times a power of two per row, and so are their weights.  Of a row,
+ * blocks below 2^-20 of its largest value lose bits, as do scales and BF16
+ * values below 2^-94.  Of a head, rows whose weight times largest value is
+ * below 2^-12 of the largest such product lose bits, and may add nothing below
+ * 2^-23 of it, even in dims where the larger rows are zero; in the denominator
+ * every row counts in full.
  *
  *   Q, O       [batch][n_q][n_heads][dim]; entries, idx, win, win_start,
  *              sink, window, m and the options as in csa_sparse_mqa_ex.
@@ -709,6 +716,8 @@ csa_status_t csa_nvfp4_linear(const void* X, const void* X_sf, const void* W, co
  *              exist and their rows of O are left as they are.
  * Entries chosen by csa_index_topk for nodes: give it the positions
  * ctx_len - 1, so that it chooses among the committed entries.
+ * options.splits: as there, rows being those below; the order in which the
+ * splits are added depends on their number alone.
  * Limits (and n_entries < 2^30) and workspace as csa_sparse_mqa_ex, with
  * csa_tree_mqa_workspace_size(rows_per_query = (k or n_entries) + window +
  * n_draft).
