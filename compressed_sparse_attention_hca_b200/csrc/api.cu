@@ -465,6 +465,7 @@ csa_status_t apply_mqa_options(csa::MqaArgs& a, const csa_mqa_options_t* opt) {
 
 csa_status_t check_mqa(const csa::MqaArgs& a) {
   REQUIRE(a.batch >= 0 && a.n_q >= 0 && a.n_entries >= 0 && a.win_len >= 0, "negative size");
+  REQUIRE((int64_t)a.batch * a.n_q < ((int64_t)1 << 31), "batch=%d x n_q=%d: too many query positions", a.batch, a.n_q);
   REQUIRE(a.m >= 1, "m=%d must be >= 1", a.m);
   REQUIRE(a.window >= 0 && a.window <= 4096, "window=%d out of range [0, 4096]", a.window);
   REQUIRE(a.n_heads >= 1 && a.n_heads <= 128, "n_heads=%d out of range [1, 128]", a.n_heads);
