@@ -499,6 +499,7 @@ csa_status_t run_mqa(csa::MqaArgs& a, void* stream, const char* name) {
                   "dim 512, n_heads a multiple of 64)");
     if (a.q_norm_g != nullptr) REQUIRE_PTR(a.q_norm_g);
   }
+  REQUIRE(csa::mqa_fits_grid(a), "batch=%d x n_q=%d x n_heads=%d: too many query positions", a.batch, a.n_q, a.n_heads);
   const size_t need = csa::mqa_workspace(a);
   REQUIRE(a.ws_bytes >= need, "workspace too small: %zu < %zu bytes", a.ws_bytes, need);
   if (need > 0) REQUIRE_PTR(a.ws);

@@ -352,6 +352,8 @@ size_t mqa_workspace(const MqaArgs& a);
 // Whether the tensor-core attention kernel takes these arguments (the query
 // normalisation and RoPE options exist only there).
 bool mqa_tc_path(const MqaArgs& a);
+// Whether the query positions and heads fit a kernel's grid.
+bool mqa_fits_grid(const MqaArgs& a);
 cudaError_t launch_mqa(const MqaArgs& a, cudaStream_t s);
 
 struct OutProjArgs {

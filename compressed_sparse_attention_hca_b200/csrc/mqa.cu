@@ -25,8 +25,11 @@ constexpr int kRC = 32;  // rows per chunk (one per lane)
 
 __global__ void __launch_bounds__(256) mqa_simt_kernel(MqaArgs a, MqaPlan plan) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  const int split = blockIdx.x, hg = blockIdx.y;
-  const int64_t bt = blockIdx.z;
+  // splits fastest, then head groups, then queries, of which there may be more
+  // than a second or third extent of a grid holds
+  const int split = (int)(blockIdx.x % (unsigned)plan.n_splits), groups = a.n_heads / plan.heads_per_cta;
+  const int64_t unit = blockIdx.x / (unsigned)plan.n_splits, bt = unit / groups;
+  const int hg = (int)(unit - bt * groups);
   const int b = (int)(bt / a.n_q);
   if (node_absent(a, bt)) return;
   const int HG = plan.heads_per_cta;
@@ -153,8 +156,8 @@ constexpr int kMaxCombineSplits = 256;
 __global__ void __launch_bounds__(128) mqa_combine_kernel(MqaArgs a, MqaPlan plan) {
   __shared__ float wgt[kMaxCombineSplits];
   __shared__ float red[4];
-  const int h = blockIdx.x;
-  const int64_t bt = blockIdx.y;
+  const int64_t bt = blockIdx.x / (unsigned)a.n_heads;
+  const int h = (int)(blockIdx.x % (unsigned)a.n_heads);
   if (node_absent(a, bt)) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float sink = a.sink[h];
@@ -243,8 +246,8 @@ __global__ void __launch_bounds__(128) mqa_combine_kernel(MqaArgs a, MqaPlan pla
 constexpr int kFewSplits = 16;
 
 __global__ void __launch_bounds__(128) mqa_combine_few_kernel(MqaArgs a, MqaPlan plan) {
-  const int h = blockIdx.x;
-  const int64_t bt = blockIdx.y;
+  const int64_t bt = blockIdx.x / (unsigned)a.n_heads;
+  const int h = (int)(blockIdx.x % (unsigned)a.n_heads);
   if (node_absent(a, bt)) return;
   const int S = plan.n_splits;
   const int d = 4 * threadIdx.x;
@@ -296,7 +299,7 @@ __global__ void __launch_bounds__(128) mqa_combine_few_kernel(MqaArgs a, MqaPlan
 }
 
 cudaError_t launch_mqa_combine(const MqaArgs& a, const MqaPlan& p, cudaStream_t s) {
-  const dim3 grid(a.n_heads, (unsigned)((int64_t)a.batch * a.n_q));
+  const unsigned grid = (unsigned)((int64_t)a.batch * a.n_q * a.n_heads);
   if (p.n_splits <= kFewSplits && a.dim % 4 == 0 && a.dim <= 512)
     mqa_combine_few_kernel<<<grid, 128, 0, s>>>(a, p);
   else
@@ -332,7 +335,7 @@ cudaError_t launch_mqa_simt(const MqaArgs& a, const MqaPlan& p, cudaStream_t s) 
   cudaError_t e = cudaFuncSetAttribute(mqa_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
   if (e != cudaSuccess) return e;
-  dim3 grid(p.n_splits, a.n_heads / p.heads_per_cta, (unsigned)((int64_t)a.batch * a.n_q));
+  const unsigned grid = (unsigned)((int64_t)a.batch * a.n_q * (a.n_heads / p.heads_per_cta) * p.n_splits);
   mqa_simt_kernel<<<grid, 32 * p.heads_per_cta, smem, s>>>(a, p);
   ++launch_counter();
   e = cudaGetLastError();
@@ -347,7 +350,14 @@ cudaError_t launch_tree_umma(const MqaArgs& a, cudaStream_t s);
 MqaPlan mqa_umma_plan(const MqaArgs& a);
 cudaError_t launch_mqa_umma(const MqaArgs& a, const MqaPlan& p, cudaStream_t s);
 
-bool mqa_tc_path(const MqaArgs& a) { return mqa_umma_path(a); }
+bool mqa_tc_path(const MqaArgs& a) { return tree_umma_path(a) || mqa_umma_path(a); }
+
+bool mqa_fits_grid(const MqaArgs& a) {
+  if (mqa_tc_path(a)) return true;
+  const MqaPlan p = make_simt_mqa_plan(a);
+  const int64_t most = (int64_t)1 << 31, bt = (int64_t)a.batch * a.n_q;  // below 2^31: checked before
+  return bt * (a.n_heads / p.heads_per_cta) * p.n_splits < most && (p.n_splits == 1 || bt * a.n_heads < most);
+}
 
 size_t mqa_workspace(const MqaArgs& a) {
   if (tree_umma_path(a)) return tree_umma_workspace(a);
