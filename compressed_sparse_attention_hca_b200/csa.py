@@ -300,6 +300,8 @@ def nvfp4_linear(X, X_sf, W, W_sf, *, alpha=1.0, out=None, out_dt=BF16, ws=None)
     """Y [T, n] = alpha X W^T of NVFP4 matrices X [T, k/2] codes and W [n, k/2]
     codes, each with blocked scales (quant_nvfp4()).  ws: a workspace of
     nvfp4_linear_workspace_size bytes; a fresh one is made when not given."""
+    if X.dim() != 2 or W.dim() != 2 or W.shape[1] != X.shape[1]:
+        raise ValueError("X must be [T, k/2] and W [n, k/2]")
     T, n = X.shape[0], W.shape[0]
     k = 2 * X.shape[1]
     if ws is None:
@@ -309,8 +311,8 @@ def nvfp4_linear(X, X_sf, W, W_sf, *, alpha=1.0, out=None, out_dt=BF16, ws=None)
     dev = _device_of(X)
     _need(dev, _U8, "codes, scales and ws", (X, X_sf, W, W_sf, ws))
     _need(dev, out.dtype, "out", (out,))
-    if 2 * W.shape[1] != k or out.shape != (T, n) or (out.dtype is not _F32 and out.dtype is not _BF16):
-        raise ValueError("X must be [T, k/2], W [n, k/2] and out [T, n] float32 or bfloat16")
+    if out.shape != (T, n) or (out.dtype is not _F32 and out.dtype is not _BF16):
+        raise ValueError("out must be [T, n] float32 or bfloat16")
     strip = k // 64 * 512
     if X_sf.numel() < (T + 127) // 128 * strip or W_sf.numel() < (n + 127) // 128 * strip:
         raise ValueError("X_sf and W_sf must be the blocked scales of X and W")

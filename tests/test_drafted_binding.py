@@ -93,3 +93,21 @@ def test_tree_refuses_query_norm_weights_of_other_sizes(lib, g, fits):
         with pytest.raises(ValueError):
             _tree(options=opt)
         assert "csa_tree_mqa" not in lib.calls
+
+
+def _linear(x, w, out=None):
+    u8 = dict(dtype=torch.uint8)
+    return csa.nvfp4_linear(torch.zeros(*x, **u8), torch.zeros(1 << 16, **u8), torch.zeros(*w, **u8),
+                            torch.zeros(1 << 16, **u8), out=out, ws=torch.zeros(256, **u8))
+
+
+def test_product_takes_matrices_only(lib):
+    """Codes of three dimensions, as quant_nvfp4 gives them for such rows, are not multiplied by their first ones."""
+    _linear((6, 64), (8, 64))
+    assert lib.calls.count("csa_nvfp4_linear") == 1
+    for x, w in (((6, 64, 64), (8, 64)), ((6, 64), (8, 64, 2)), ((64,), (8, 64)), ((6, 64), (64,)), ((6, 64), (8, 32))):
+        with pytest.raises(ValueError):
+            _linear(x, w)
+    with pytest.raises(ValueError):
+        _linear((6, 64), (8, 64), out=torch.zeros(8, 6))
+    assert lib.calls.count("csa_nvfp4_linear") == 1
