@@ -489,7 +489,7 @@ csa_status_t run_mqa(csa::MqaArgs& a, void* stream, const char* name) {
   REQUIRE_PTR(a.sink);
   if (a.n_entries > 0) REQUIRE_PTR(a.entries);
   if (a.window > 0) {
-    REQUIRE_PTR(a.win);
+    if (a.win_len > 0 || a.ctx_len == nullptr) REQUIRE_PTR(a.win);  // a tree may have nothing committed
     REQUIRE_PTR(a.win_start);
   }
   if (a.q_norm_g != nullptr || a.q_rope_dims > 0 || a.out_rope_dims > 0) {

@@ -708,6 +708,7 @@ csa_status_t csa_nvfp4_linear(const void* X, const void* X_sf, const void* W, co
  *
  *   Q, O       [batch][n_q][n_heads][dim]; entries, idx, win, win_start,
  *              sink, window, m and the options as in csa_sparse_mqa_ex.
+ *              win may be NULL with win_len 0 (nothing committed yet).
  *   draft      [batch][n_draft] rows of kv_dt (n_draft <= 1024; NULL when 0).
  *   tree_mask  [batch][n_q][ceil(n_draft / 32)] uint32 (device).
  *   ctx_len    [batch] int64 (device): committed tokens.
