@@ -27,6 +27,7 @@ csa_status_t ok() {
 
 csa_status_t cuda_status(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return ok();
+  cudaGetLastError();  // taken: the next call that launches would report it again
   return fail(CSA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
