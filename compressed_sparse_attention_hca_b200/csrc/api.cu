@@ -483,7 +483,8 @@ csa_status_t run_mqa(csa::MqaArgs& a, void* stream, const char* name) {
   g_launches = 0;
   csa_status_t st = check_mqa(a);
   if (st != CSA_OK) return st;
-  if ((int64_t)a.batch * a.n_q == 0) return ok();
+  if ((int64_t)a.batch * a.n_q == 0)  // the compression, if there is one
+    return cuda_status(csa::launch_mqa(a, static_cast<cudaStream_t>(stream)), name);
   REQUIRE_PTR(a.Q);
   REQUIRE_PTR(a.O);
   REQUIRE_PTR(a.q_pos);
