@@ -17,10 +17,11 @@
 // request that gives back a few places the thread that reads its lengths, of
 // one that gives back many all warps, 256 places at a time.
 //
-// Latency bounds it: a step of 256 requests takes 6.5 us (a launch ~2.5, then
-// four or five dependent reads and the scan), 16 prompts of 131,072 to 262,144
-// tokens 11.7 us for 7 MB of slots.  Code comes cold from the instruction cache,
-// so loops are not unrolled (7.1 and 12.1 us with the compiler's choice).
+// Latency bounds it: a step of 256 requests takes 6.4 us (a launch ~2.5, then
+// four or five dependent reads and the scan), one that rolls back 4.4 (4.1
+// without the count of pages), 16 prompts of 131,072 to 262,144 tokens 14.2 us
+// for 8 MB of slots (13.6).  Code comes cold from the instruction cache, so loops are
+// not unrolled (the compiler's choice took 4 to 9 % longer).
 #include "csa_internal.cuh"
 #include "sm100.cuh"
 
